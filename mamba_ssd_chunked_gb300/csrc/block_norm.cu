@@ -468,7 +468,9 @@ __device__ __forceinline__ void walk_rows(const NormParams<T, TR>& p, const Ring
 template <typename T, typename TR, int V, int R>
 __global__ void __launch_bounds__(ring_threads(V, R, false), 1) block_norm_fwd_ring(const NormParams<T, TR> p, const RingShape g) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float bufs[16][2][32];
+    // The first sum's two take turns by row: without a pre-norm it is a row's only barrier, and a fast
+    // warp writes the next row's part while a slow one still adds up this row's. The second sum has its own.
+    __shared__ float bufs[16][3][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / p.warps_per_row, in_group = warp - group * p.warps_per_row;
     const int tid = in_group * 32 + lane, stride = p.warps_per_row * 32;
@@ -486,6 +488,7 @@ __global__ void __launch_bounds__(ring_threads(V, R, false), 1) block_norm_fwd_r
             for (int i = 0; i < V; ++i) c[k][i] *= s[i];
         }
     }
+    int turn = 0;
     walk_rows<T, TR, false, (V <= 2)>(p, g, smem, [&](long long row, const auto& ring, const unsigned char* st, auto release) {
         float u[R][V], r[R][V], su[1] = {0.f};
 #pragma unroll
@@ -510,7 +513,8 @@ __global__ void __launch_bounds__(ring_threads(V, R, false), 1) block_norm_fwd_r
                 }
             }
         }
-        group_sum<1>(su, bufs[group][0], p.warps_per_row, in_group, lane, 1 + group);
+        group_sum<1>(su, bufs[group][turn], p.warps_per_row, in_group, lane, 1 + group);
+        turn ^= 1;
         release();
         const float rho_u = p.post ? rsqrtf(fmaf(su[0], inv, p.eps)) : 1.f;
         float sr[1] = {0.f};
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(ring_threads(V, R, false), 1) block_norm_fwd_r
         }
         float rho = 1.f;
         if (p.pre) {
-            group_sum<1>(sr, bufs[group][1], p.warps_per_row, in_group, lane, 1 + group);
+            group_sum<1>(sr, bufs[group][2], p.warps_per_row, in_group, lane, 1 + group);
             rho = rsqrtf(fmaf(sr[0], inv, p.eps));
 #pragma unroll
             for (int k = 0; k < R; ++k) {
