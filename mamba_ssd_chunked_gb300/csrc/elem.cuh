@@ -165,8 +165,8 @@ template <int V>
 __device__ __forceinline__ Vals<V> exp2_fast(Vals<V> a) {
     return each<V>(a, [](float v) { return exp2_fast(v); });
 }
-// e^v for v <= 0. Near 1, where a long product of such factors adds up their errors, the
-// series 1 + v + v^2/2 + v^3/6 + v^4/24 (exact to 2^-26 for v > -1/16) rounds once; exp2_fast's
+// e^v, v of either sign. Near 1, where a long product of such factors adds up their errors, the
+// series 1 + v + v^2/2 + v^3/6 + v^4/24 (exact to 2^-26 for |v| < 1/16) rounds once; exp2_fast's
 // error of up to 2^-22 showed in the gradients of slowly decaying states.
 template <int V>
 __device__ __forceinline__ Vals<V> exp_near(Vals<V> v) {
@@ -177,9 +177,9 @@ __device__ __forceinline__ Vals<V> exp_near(Vals<V> v) {
     s = fma(s, v, L::splat(1.f));
     s = fma(s, v, L::splat(1.f));
     if constexpr (V == 1)
-        return {v.f > -0.0625f ? s.f : e.f};
+        return {fabsf(v.f) < 0.0625f ? s.f : e.f};
     else
-        return L::make(v.get(0) > -0.0625f ? s.get(0) : e.get(0), v.get(1) > -0.0625f ? s.get(1) : e.get(1));
+        return L::make(fabsf(v.get(0)) < 0.0625f ? s.get(0) : e.get(0), fabsf(v.get(1)) < 0.0625f ? s.get(1) : e.get(1));
 }
 template <typename T, int V>
 __device__ __forceinline__ Vals<V> unpack(const Pack<T, V>& k) {

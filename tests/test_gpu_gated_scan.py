@@ -365,3 +365,26 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
     monkeypatch.delenv("SSD_DEVICE_WAIT_NS")
     got, _, _ = pkg.ssd_gated_scan(*args, init_state=t["init"])
     assert pkg.ssd_device_status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_decays_above_one(io):
+    """A of either sign, and zero: forward, gradients and decode steps. delta is below 1.5 and A at most 0.5, so an
+    exponent delta A below 0.75 carries delta's 2^-22: a step's decay stays within the 2^-21 of the bound."""
+    import mamba_ssd_chunked_gb300 as pkg
+    b, L, d = 2, 41, 70
+    t = make(b, L, d, DTYPES[io], seed=20)
+    t["dt"] = t["dt"].clamp(max=1.0)
+    t["dt_bias"] = t["dt_bias"].clamp(max=0.2)
+    t["dt_bias"][:8] = 0.2
+    t["A"] = torch.linspace(-1.0, 0.05, d, device="cuda")
+    t["A"][:6], t["A"][6], t["A"][7] = 0.5, 0.0, 0.1
+    check(run(t), t, io)
+    ref, most = reference(t), reference(t, absolute=True)
+    state = t["init"].clone()
+    r = 2.0 ** -8 if io == "bf16" else 2.0 ** -23
+    for i in range(L):
+        y = pkg.ssd_gated_scan_step(t["x"][:, i], t["dt"][:, i], t["dt_bias"], t["A"], t["D"], state=state)
+        bound = (2 * L + 32) * 2.0 ** -21 * most["y"][:, i] + r * ref["y"][:, i].abs()
+        assert ((y.double() - ref["y"][:, i]).abs() <= bound).all()
+    assert ((state.double() - ref["final_state"]).abs() <= (2 * L + 32) * 2.0 ** -21 * most["final_state"]).all()
