@@ -562,7 +562,8 @@ SSD_API size_t ssd_block_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
  *
  * Products of bf16 operands, and of fp32 ones as sums of three bf16 terms, accumulate
  * in fp32; the softmax statistics are fp32 and joined in a fixed order. Rows of 16-byte aligned starts (dim a
- * multiple of 8, dense, bf16) are read in place, others packed into the workspace first.
+ * multiple of 8, dense, bf16) are read in place, others packed into the workspace first (a weight that only
+ * starts off 16 bytes in pieces, of 64 MB or of 256 classes if those are more).
  * Errors: SSD_ERR_INVALID_ARG (NULL, sizes < 1, stride < dim), SSD_ERR_UNSUPPORTED
  * (misaligned elements, sizes beyond the indexing limits), SSD_ERR_WORKSPACE.
  * Asynchronous on `stream`.

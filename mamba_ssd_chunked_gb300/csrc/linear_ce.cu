@@ -80,7 +80,7 @@ struct CeParams {
     int segs;     // 1 (bf16), or the six products of three-term operands
     int seg_a[kMaxSegs], seg_b[kMaxSegs];
     long long rows, vocab, dim;
-    int v0, v1;  // the piece's vocabulary range
+    int v0, v1;  // the piece's vocabulary range (v0: a whole number of tiles)
     const long long* target;
     long long ignore;
     // kStats
@@ -316,14 +316,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 __device__ __forceinline__ void epilogue_stats(const EpiTile& e) {
     const CeParams& p = e.p;
-    const long long col0 = static_cast<long long>(e.t.n) * kTileN + e.half * kEpiCols;
+    const long long col0 = p.v0 + static_cast<long long>(e.t.n) * kTileN + e.half * kEpiCols;
     const long long target = e.row < p.rows ? p.target[e.row] : -1;
     float m = -__builtin_inff(), s = 0.f;
 #pragma unroll 1
     for (int c = 0; c < kEpiCols; c += 32) {
         uint32_t r[32];
         e.load(c, r);
-        const int left = within64(p.vocab - (col0 + c));
+        const int left = within64(p.v1 - (col0 + c));
         if (left <= 0) continue;
         if (left < 32) {
 #pragma unroll
@@ -350,7 +350,7 @@ __device__ __forceinline__ void epilogue_stats(const EpiTile& e) {
             p.picked[e.row] = v;
         }
     }
-    if (e.row < p.rows) p.stats[(2ll * e.t.n + e.half) * p.rows + e.row] = make_float2(m, s);
+    if (e.row < p.rows) p.stats[(2ll * (p.v0 / kTileN + e.t.n) + e.half) * p.rows + e.row] = make_float2(m, s);
 }
 
 // What dl is held relative to: the first row's dloss, where it is of a magnitude that
@@ -951,6 +951,7 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- host side
 constexpr long long kPieceBytes = 256ll << 20;  // dl of one piece, at most (one tile's width at least)
+constexpr long long kWeightBytes = 64ll << 20;  // of a weight that is packed in pieces, likewise
 
 long long up(long long v, long long m) { return (v + m - 1) / m * m; }
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -962,15 +963,21 @@ constexpr int kFewRows = 32;
 constexpr int kFlush = 8;
 int pair_count() { return std::max(1, device_sms() / 2); }
 
+// How the products read the weight: as it is; as a copy; or, where only its first element's
+// address is in the way (bf16, dim a multiple of 8), as copies of one piece of the vocabulary after another, so
+// that the workspace need not hold a copy of a weight that nearly always lies right.
+enum Weight { kInPlace, kPacked, kPieces };
+
 // Everything that follows from the sizes. Operands are packed where TMA cannot read
 // them in place: fp32, or rows that do not start on 16 bytes.
 struct CePlan {
     bool few;      // the forward of few fp32 rows: no packing, statistics of kFewV classes
+    Weight form;
     long long ld;  // packed rows
-    int planes, segs, piece, splits;
+    int planes, segs, piece, splits;  // (piece of the forward: the whole vocabulary but in kPieces)
     size_t hidden, weight, stats, picked, dl, acc, total;
 };
-CePlan ce_plan(long long rows, long long dim, long long vocab, ssd_dtype io, bool backward, bool pack_h, bool pack_w,
+CePlan ce_plan(long long rows, long long dim, long long vocab, ssd_dtype io, bool backward, bool pack_h, Weight form,
                int pairs) {
     CePlan c{};
     c.ld = up(dim, 8);
@@ -983,15 +990,20 @@ CePlan ce_plan(long long rows, long long dim, long long vocab, ssd_dtype io, boo
         return r;
     };
     c.few = !backward && io == SSD_F32 && rows <= kFewRows;
-    if (c.few) pack_h = pack_w = false;
+    if (c.few) pack_h = false, form = kInPlace;
+    c.form = form;
+    const long long all = up(vocab, kTileN) / kTileN;  // tiles
+    long long most = all;                              // and of one piece
+    if (form == kPieces) most = std::min(all, std::max<long long>(1, kWeightBytes / (2 * c.ld * kTileN)));
     c.hidden = take(pack_h ? 2 * c.planes * rows * c.ld : 0);
-    c.weight = take(pack_w ? 2 * c.planes * vocab * c.ld : 0);
+    c.weight = take(form == kInPlace ? 0 : 2 * c.planes * std::min(vocab, most * kTileN) * c.ld);
     if (!backward) {
+        c.piece = static_cast<int>(most * kTileN);
         c.stats = take(8 * (c.few ? up(vocab, kFewV) / kFewV : 2 * (up(vocab, kTileN) / kTileN)) * rows);
         c.picked = take(4 * rows);
     } else {
-        const long long most = std::max<long long>(1, kPieceBytes / (2ll * c.planes * rows * kTileN));  // tiles
-        const long long all = up(vocab, kTileN) / kTileN, pieces = (all + most - 1) / most;
+        most = std::min(most, std::max<long long>(1, kPieceBytes / (2ll * c.planes * rows * kTileN)));
+        const long long pieces = (all + most - 1) / most;
         c.piece = static_cast<int>((all + pieces - 1) / pieces * kTileN);  // even pieces
         const long long tiles = up(rows, kTileM) / kTileM * (up(dim, kTileN) / kTileN);
         c.splits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.planes > 1 ? 2 : 1) * pairs / tiles, c.piece / kBK / 4)));
@@ -1062,7 +1074,17 @@ struct Operands {
 bool in_place(const void* p, long long stride, const CeCall& c) {
     return c.io == SSD_BF16 && c.dim % 8 == 0 && stride == c.dim && aligned_to(p, 16);
 }
-Operands lay_out(const CeCall& c, const CePlan& pl, bool pack_h, bool pack_w, bool drop) {
+Weight weight_form(const CeCall& c) {
+    return in_place(c.weight, c.dim, c) ? kInPlace : c.io == SSD_BF16 && c.dim % 8 == 0 ? kPieces : kPacked;
+}
+// Rows [v0, v1) of the weight into the workspace, once nothing reads what is there (kPieces).
+const void* pack_piece(const CeCall& c, const CePlan& pl, long long v0, long long v1) {
+    void* dst = c.ws + pl.weight;
+    pack<__nv_bfloat16>(false, static_cast<const __nv_bfloat16*>(c.weight) + v0 * c.dim, c.dim, v1 - v0, false, c, pl, dst);
+    return dst;
+}
+Operands lay_out(const CeCall& c, const CePlan& pl, bool pack_h, bool drop) {
+    const bool pack_w = pl.form == kPacked;
     Operands o{c.hidden, c.weight, c.dim, c.dim};
     auto one = [&](bool after, const void* src, long long stride, long long rows, bool zero, size_t at) -> const void* {
         void* dst = c.ws + at;
@@ -1110,25 +1132,32 @@ ssd_status check_ce(ssd_dtype io, int64_t rows, int64_t dim, int64_t vocab) {
     return SSD_OK;
 }
 
-ssd_status tile_stats(const CeCall& c, const CePlan& pl, bool pack_h, bool pack_w, int pairs) {
+ssd_status tile_stats(const CeCall& c, const CePlan& pl, bool pack_h, int pairs) {
     CeParams p;
     ssd_status st = base_params(c, pl, &p);
     if (st != SSD_OK) return st;
-    const Operands o = lay_out(c, pl, pack_h, pack_w, false);
-    Maps m{};
-    if (!make_map_bf16(&m.a0, o.h, o.h_ld, 1, c.rows, pl.planes, 64) ||
-        !make_map_bf16(&m.b0, o.w, o.w_ld, 1, c.vocab, pl.planes, 64))
-        return SSD_ERR_CUDA;
-    m.a1 = m.a0, m.b1 = m.b0;
-    p.v0 = 0, p.v1 = static_cast<int>(c.vocab);
+    const Operands o = lay_out(c, pl, pack_h, false);
+    const bool pieces = pl.form == kPieces;
     p.stats = reinterpret_cast<float2*>(c.ws + pl.stats);
     p.picked = reinterpret_cast<float*>(c.ws + pl.picked);
-    Product& q = p.prod[0];
-    q.tiles_m = static_cast<int>(up(c.rows, kTileM) / kTileM);
-    q.tiles_n = static_cast<int>(up(c.vocab, kTileN) / kTileN);
-    q.splits = 1, q.blocks = static_cast<int>(up(pl.ld, kBK) / kBK), q.m_fast = 1;
-    p.jobs[0] = q.tiles_m * q.tiles_n;
-    return launch_gemm<kStats>(pack_h || pack_w, m, p, pairs, c.stream);
+    for (long long v0 = 0; v0 < c.vocab; v0 += pl.piece) {
+        const long long v1 = std::min<long long>(c.vocab, v0 + pl.piece);
+        const void* w = pieces ? pack_piece(c, pl, v0, v1) : o.w;
+        Maps m{};
+        if (!make_map_bf16(&m.a0, o.h, o.h_ld, 1, c.rows, pl.planes, 64) ||
+            !make_map_bf16(&m.b0, w, o.w_ld, 1, v1 - v0, pl.planes, 64))
+            return SSD_ERR_CUDA;
+        m.a1 = m.a0, m.b1 = m.b0;
+        p.v0 = static_cast<int>(v0), p.v1 = static_cast<int>(v1);
+        Product& q = p.prod[0];
+        q.tiles_m = static_cast<int>(up(c.rows, kTileM) / kTileM);
+        q.tiles_n = static_cast<int>(up(v1 - v0, kTileN) / kTileN);
+        q.splits = 1, q.blocks = static_cast<int>(up(pl.ld, kBK) / kBK), q.m_fast = 1;
+        p.jobs[0] = q.tiles_m * q.tiles_n;
+        st = launch_gemm<kStats>(pack_h || pl.form != kInPlace, m, p, pairs, c.stream);
+        if (st != SSD_OK) return st;
+    }
+    return SSD_OK;
 }
 
 template <int RP>
@@ -1144,7 +1173,7 @@ ssd_status few_stats(const CeCall& c, const CePlan& pl, bool vec) {
 }
 
 // Statistics of all logits, then loss and lse from them.
-ssd_status ce_forward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack_w, float* loss, float* lse, int pairs) {
+ssd_status ce_forward(const CeCall& c, const CePlan& pl, bool pack_h, float* loss, float* lse, int pairs) {
     const bool vec = whole16(c.hidden, c.hs, c) && whole16(c.weight, c.dim, c);
     int parts;
     ssd_status st;
@@ -1153,7 +1182,7 @@ ssd_status ce_forward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack_
         st = c.rows <= 8 ? few_stats<8>(c, pl, vec) : c.rows <= 16 ? few_stats<16>(c, pl, vec) : few_stats<32>(c, pl, vec);
     } else {
         parts = static_cast<int>(2 * (up(c.vocab, kTileN) / kTileN));
-        st = tile_stats(c, pl, pack_h, pack_w, pairs);
+        st = tile_stats(c, pl, pack_h, pairs);
     }
     if (st != SSD_OK) return st;
     const unsigned grid = static_cast<unsigned>((c.rows + kLseRows - 1) / kLseRows);
@@ -1170,12 +1199,13 @@ ssd_status ce_forward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack_
     return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
-ssd_status ce_backward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack_w, const float* dloss, const float* lse,
-                       void* dhidden, void* dweight, int pairs) {
+ssd_status ce_backward(const CeCall& c, const CePlan& pl, const float* dloss, const float* lse, void* dhidden, void* dweight,
+                       int pairs) {
     CeParams p;
     ssd_status st = base_params(c, pl, &p);
     if (st != SSD_OK) return st;
-    const Operands o = lay_out(c, pl, pack_h, pack_w, true);
+    const Operands o = lay_out(c, pl, true, true);
+    const bool pieces = pl.form == kPieces;
     p.lse = lse, p.dloss = dloss, p.acc_ld = pl.ld;
     void* dl = c.ws + pl.dl;
     float* acc = reinterpret_cast<float*>(c.ws + pl.acc);
@@ -1184,12 +1214,10 @@ ssd_status ce_backward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack
     Maps logits{}, grads{};
     // The logits come from hidden itself where they can (a row without a loss has none that count):
     // their kernel then runs beside the packing.
-    const bool beside = in_place(c.hidden, c.hs, c) && !pack_w;
+    const bool beside = in_place(c.hidden, c.hs, c) && pl.form == kInPlace;
     if (!make_map_bf16(&logits.a0, beside ? c.hidden : o.h, beside ? c.dim : o.h_ld, 1, c.rows, pl.planes, 64) ||
-        !make_map_bf16(&logits.b0, o.w, o.w_ld, 1, c.vocab, pl.planes, 64) ||
         !make_map_bf16(&logits.out, dl, pl.piece, 1, c.rows, pl.planes, 32) ||
         !make_map_bf16(&grads.a0, dl, pl.piece, 1, c.rows, pl.planes, 64) ||
-        !make_map_bf16(&grads.b0, o.w, o.w_ld, 1, c.vocab, pl.planes, 64) ||
         !make_map_bf16(&grads.a1, dl, pl.piece, 1, c.rows, pl.planes, 64) ||
         !make_map_bf16(&grads.b1, o.h, o.h_ld, 1, c.rows, pl.planes, 64) ||
         !make_map_f32(&grads.out, acc, pl.ld, 1, c.rows, pl.splits, 32))
@@ -1197,7 +1225,7 @@ ssd_status ce_backward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack
     if (p.dw_vec && !(p.dw_f32 ? make_map_f32(&grads.dw, dweight, c.dim, 1, c.vocab, 1, 32)
                                : make_map_bf16(&grads.dw, dweight, c.dim, 1, c.vocab, 1, 32)))
         return SSD_ERR_CUDA;
-    logits.a1 = logits.a0, logits.b1 = logits.b0;
+    logits.a1 = logits.a0;
     if (pl.planes > 1) {
         p.picked = reinterpret_cast<float*>(c.ws + pl.picked);
         launch(true, ce_targets, static_cast<unsigned>((c.rows + 7) / 8), 256, 0, c.stream,
@@ -1210,10 +1238,16 @@ ssd_status ce_backward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack
         const long long v1 = std::min<long long>(c.vocab, v0 + pl.piece);
         const int tiles_v = static_cast<int>(up(v1 - v0, kTileN) / kTileN);
         p.v0 = static_cast<int>(v0), p.v1 = static_cast<int>(v1), p.first = v0 == 0;
+        if (v0 == 0 || pieces) {
+            const void* w = pieces ? pack_piece(c, pl, v0, v1) : o.w;
+            if (!make_map_bf16(&logits.b0, w, o.w_ld, 1, pieces ? v1 - v0 : c.vocab, pl.planes, 64)) return SSD_ERR_CUDA;
+            grads.b0 = logits.b1 = logits.b0;
+        }
+        const int w_row = pieces ? 0 : p.v0;
         CeParams a = p;
         Product& q = a.prod[0];
         q = Product{};
-        q.b_row = p.v0;
+        q.b_row = w_row;
         q.tiles_m = tiles_r, q.tiles_n = tiles_v, q.splits = 1;
         q.blocks = static_cast<int>(up(pl.ld, kBK) / kBK), q.m_fast = 1;
         a.jobs[0] = tiles_r * tiles_v;
@@ -1222,7 +1256,7 @@ ssd_status ce_backward(const CeCall& c, const CePlan& pl, bool pack_h, bool pack
         if (st != SSD_OK) return st;
         CeParams b = p;
         Product& dh = b.prod[0];  // [rows, dim] = dl [rows, piece] weight [piece, dim]
-        dh.b_mn = 1, dh.b_dep = p.v0;
+        dh.b_mn = 1, dh.b_dep = w_row;
         dh.tiles_m = tiles_r, dh.tiles_n = tiles_d, dh.splits = pl.splits;
         dh.blocks = tiles_v * (kTileN / kBK);
         b.jobs[0] = tiles_r * tiles_d * pl.splits;
@@ -1267,8 +1301,10 @@ extern "C" {
 size_t ssd_linear_cross_entropy_workspace_bytes(ssd_dtype io_dtype, int64_t rows, int64_t dim, int64_t vocab, int backward) {
     using namespace ssd;
     if (check_ce(io_dtype, rows, dim, vocab) != SSD_OK) return 0;
-    return ce_plan(rows, dim, vocab, io_dtype, backward != 0, true, io_dtype == SSD_F32 || dim % 8 != 0, pair_count())
-        .total;
+    const int pairs = pair_count();
+    auto bytes = [&](Weight form) { return ce_plan(rows, dim, vocab, io_dtype, backward != 0, true, form, pairs).total; };
+    if (io_dtype == SSD_F32 || dim % 8 != 0) return bytes(kPacked);
+    return std::max(bytes(kInPlace), bytes(kPieces));  // wherever the weight starts
 }
 
 ssd_status ssd_linear_cross_entropy(ssd_dtype io_dtype, int64_t rows, int64_t dim, int64_t vocab, const void* hidden,
@@ -1283,11 +1319,11 @@ ssd_status ssd_linear_cross_entropy(ssd_dtype io_dtype, int64_t rows, int64_t di
     const CeCall c{rows, dim, vocab, io_dtype, hidden, hidden_row_stride, weight,
                    reinterpret_cast<const long long*>(target), ignore_index, static_cast<char*>(workspace),
                    static_cast<cudaStream_t>(stream)};
-    const bool pack_h = !in_place(hidden, hidden_row_stride, c), pack_w = !in_place(weight, dim, c);
+    const bool pack_h = !in_place(hidden, hidden_row_stride, c);
     const int pairs = pair_count();
-    const CePlan pl = ce_plan(rows, dim, vocab, io_dtype, false, pack_h, pack_w, pairs);
+    const CePlan pl = ce_plan(rows, dim, vocab, io_dtype, false, pack_h, weight_form(c), pairs);
     if (!workspace || !aligned_to(workspace, kWorkspaceAlign) || workspace_bytes < pl.total) return SSD_ERR_WORKSPACE;
-    return ce_forward(c, pl, pack_h, pack_w, loss, lse, pairs);
+    return ce_forward(c, pl, pack_h, loss, lse, pairs);
 }
 
 ssd_status ssd_linear_cross_entropy_bwd(ssd_dtype io_dtype, int64_t rows, int64_t dim, int64_t vocab, const float* dloss,
@@ -1303,11 +1339,10 @@ ssd_status ssd_linear_cross_entropy_bwd(ssd_dtype io_dtype, int64_t rows, int64_
     const CeCall c{rows, dim, vocab, io_dtype, hidden, hidden_row_stride, weight,
                    reinterpret_cast<const long long*>(target), ignore_index, static_cast<char*>(workspace),
                    static_cast<cudaStream_t>(stream)};
-    const bool pack_h = true, pack_w = !in_place(weight, dim, c);
     const int pairs = pair_count();
-    const CePlan pl = ce_plan(rows, dim, vocab, io_dtype, true, pack_h, pack_w, pairs);
+    const CePlan pl = ce_plan(rows, dim, vocab, io_dtype, true, true, weight_form(c), pairs);
     if (!workspace || !aligned_to(workspace, kWorkspaceAlign) || workspace_bytes < pl.total) return SSD_ERR_WORKSPACE;
-    return ce_backward(c, pl, pack_h, pack_w, dloss, lse, dhidden, dweight, pairs);
+    return ce_backward(c, pl, dloss, lse, dhidden, dweight, pairs);
 }
 
 }  // extern "C"
