@@ -5,9 +5,12 @@
 Each runs its forward and its gradients in the library's kernels (ssd_gated_scan and
 _bwd, ssd_block_norm and _bwd, ssd_linear_cross_entropy and _bwd), with their
 arguments, layouts and errors. What a gradient needs is kept by torch's graph.
-Gradients that reach an operator non-contiguous are copied once.
+Gradients that reach an operator non-contiguous are copied once. The gradients
+have no derivative of their own: differentiating them again raises.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
@@ -21,6 +24,33 @@ def _dense(t, dtype):
     return None if t is None else t.to(dtype).contiguous()
 
 
+class _Final(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad, name, *depends_on):
+        ctx.name = name
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name}: its gradients cannot be differentiated again")
+
+
+def _first_order(name):
+    """Decorates a backward whose results depend on the operator's inputs in ways that torch does not see. Under
+    create_graph they would count as constants; here whoever differentiates them gets an error."""
+    def wrap(backward):
+        @functools.wraps(backward)
+        def run(ctx, *grads):
+            with torch.no_grad():
+                out = backward(ctx, *grads)
+            if not torch.is_grad_enabled():
+                return out
+            on = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+            return tuple(None if g is None else _Final.apply(g, name, *on) for g in out)
+        return run
+    return wrap
+
+
 class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, dt_bias, A, D, init_state, seq_idx):
@@ -32,6 +62,7 @@ class _GatedScan(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @_first_order("gated_scan")
     def backward(ctx, dy, dfinal):
         x, dt, dt_bias, A, D, seq_idx, chunks = ctx.saved_tensors
         dy = torch.zeros_like(x, memory_format=torch.contiguous_format) if dy is None else _dense(dy, x.dtype)
@@ -51,6 +82,7 @@ class _BlockNorm(torch.autograd.Function):
         return r, out
 
     @staticmethod
+    @_first_order("block_norm")
     def backward(ctx, dr, dout):
         y, residual, z, post_weight, scale, pre_weight, rstd = ctx.saved_tensors
         if pre_weight is not None and dout is None:
@@ -73,6 +105,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         return loss, lse
 
     @staticmethod
+    @_first_order("linear_cross_entropy")
     def backward(ctx, dloss, _):
         hidden, weight, target, lse = ctx.saved_tensors
         dh, dw = ssd_linear_cross_entropy_bwd(_dense(dloss, torch.float32), hidden, weight, target, lse,
