@@ -426,6 +426,7 @@ typedef struct {
  *
  *   delta[b,t,c] = softplus(dt[b,t,c] + dt_bias[c])
  *   a[b,t,c]     = exp(delta[b,t,c] A[c]);  0 where seq_idx[b,t] != seq_idx[b,t-1], t > 0
+ *                  (there nothing passes, in either direction: no infinity and no NaN)
  *   h_t          = a_t h_{t-1} + delta_t x_t,   h_{-1} = init_state (zeros when NULL)
  *   y_t          = h_t + D[c] x_t               (D == NULL: no skip)
  *

@@ -563,7 +563,7 @@ def ssd_gated_scan(x, dt, dt_bias, A, D=None, init_state=None, seq_idx=None, ret
     [b, L, d] (CUDA, bf16 or fp32 alike, last dim contiguous, tokens packed at a
     row stride, e.g. slices of a projection), dt_bias, A and D [d] fp32, init_state
     [b, d] fp32, seq_idx [b, L] int32 (the state restarts from zero wherever it
-    changes between consecutive tokens of a row):
+    changes between consecutive tokens of a row; an infinity or NaN stays in its sequence):
 
         delta = softplus(dt + dt_bias);  h_t = exp(delta A) h_{t-1} + delta x_t;  y = h + D x
 

@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <cstddef>
 #include <initializer_list>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "ptx.cuh"
@@ -176,12 +177,30 @@ __device__ __forceinline__ Map compose(Map then, Map first) {
 __device__ __forceinline__ Pair apply(Map m, Pair s) {
     return elem::fma(m.P, s, m.q);
 }
+// Packed sequences (kSeq): where one begins nothing of the one before passes. A zero in the place of
+// the decay would not do: zero times an infinity or a NaN of the other sequence is NaN. A run with such a
+// token (Slot::cut_runs) maps every s to q, and maps are composed from the last such run on; a published
+// tile's P is then -0, which no product of decays is (none of them is negative). The guide looks seq_idx up
+// with the tile. 4 x 4096 x 5120 (bf16) in sequences of 300 tokens: forward 134 us (126 unpacked), backward 279 (252);
+// 1 x 131072 x 4096: 787 (736) and 1735 (1555).
+__device__ __forceinline__ Pair cut_P() { return Pair::splat(-0.f); }
+__device__ __forceinline__ bool is_cut(Pair P) { return __float_as_uint(P.get(0)) == 0x80000000u; }  // (both channels alike)
+// f(std::true_type) or f(std::false_type); kMay: `yes` may be true
+template <bool kMay, typename F>
+__device__ __forceinline__ void with(bool yes, F f) {
+    if (kMay && yes)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
+}
 
 // A tile as the computing warps see it, looked up three tiles ahead by the guiding warp.
 struct Slot {
     int step, b;     // step counts tiles in scan order; -1: no more tiles
     long long c0;    // first channel
     Pair A[32], bias[32], D[32], state[32];  // (state: backward only)
+    // packed sequences: a bit for each token of the tile that begins one, and for each run with such a token
+    uint32_t begins[8], cut_runs;
 };
 
 // Live at once: the finished tile whose sums are stored, the current one, and three ahead.
@@ -200,6 +219,13 @@ struct Exchange {
     Pair f[2][kWarps<T>][32];        // the forward maps' constants (their P is run's)
     Pair sums[2][3][kWarps<T>][32];  // dA, d dt_bias, dD
 };
+
+// The last of the runs before `run`, and the first after it, that is among `cuts` (-1: none).
+__device__ __forceinline__ int last_before(uint32_t cuts, int run) { return 31 - __clz(cuts & ((1u << run) - 1u)); }
+__device__ __forceinline__ int first_after(uint32_t cuts, int run) {
+    const int ahead = __ffs(cuts >> run >> 1);
+    return ahead == 0 ? -1 : run + ahead;
+}
 
 // One thread's channels. A lane past the last channel computes on whatever is there and
 // writes nothing.
@@ -222,11 +248,13 @@ __device__ __forceinline__ Place place_in(const ScanParams<T>& p, const Slot& t)
 
 // ---------------------------------------------------------------- the guiding warp
 // Tile `unit`, looked up.
-template <typename T, bool kAny, bool kForward>
+template <typename T, bool kAny, bool kForward, bool kSeq>
 struct Lookup {
+    static constexpr int kRun = kForward ? kRunFwd<T> : kRunBwd, kTile = kRun * kWarps<T>, kWords = (kTile + 31) / 32;
     int step, b;
     long long c0;
     Pair A, bias, D, state;
+    uint32_t begins[kWords], cut_runs;
     __device__ __forceinline__ void fetch(const ScanParams<T>& p, int unit, int lane) {
         step = -1;
         if (unit >= p.chains * p.tiles) return;
@@ -244,11 +272,35 @@ struct Lookup {
             if (!kForward)
                 state = load_pair<kAny>(p.states + (static_cast<long long>(b) * p.tiles + (p.tiles - 1 - step)) * p.dim + c, both);
         }
+        if constexpr (kSeq) {
+            const long long t0 = static_cast<long long>(kForward ? step : p.tiles - 1 - step) * kTile;
+            const int* seq = p.seq + b * p.L + t0;
+            int here[kWords], last[kWords];
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                const int i = k * 32 + lane;
+                here[k] = last[k] = 0;
+                if (i < kTile && t0 + i > 0 && t0 + i < p.L) here[k] = __ldg(seq + i), last[k] = __ldg(seq + i - 1);
+            }
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) begins[k] = __ballot_sync(0xffffffffu, here[k] != last[k]);
+            cut_runs = 0u;
+#pragma unroll
+            for (int k = 0; k < kWarps<T>; ++k)
+                if (begins[k * kRun / 32] >> k * kRun % 32 & ((1u << kRun) - 1u)) cut_runs |= 1u << k;
+        }
     }
     __device__ __forceinline__ void store(Slot& t, int lane) const {
         if (lane == 0) t.step = step, t.b = b, t.c0 = c0;
         t.A[lane] = A, t.bias[lane] = bias, t.D[lane] = D;
         if (!kForward) t.state[lane] = state;
+        if constexpr (kSeq) {
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) t.begins[k] = begins[k];
+                t.cut_runs = cut_runs;
+            }
+        }
     }
 };
 
@@ -287,6 +339,7 @@ struct Incoming {
             if (live && k < n) yes = yes && all_set(m[k]);
         return yes;
     }
+    template <bool kSeq>
     __device__ __forceinline__ Pair value(const ScanParams<T>& p, const Place& w) const {
         Pair s = Pair::splat(0.f);
         if (!live) return s;
@@ -296,23 +349,31 @@ struct Incoming {
             s = load_pair<kAny>(p.init + w.own, w.both);
 #pragma unroll
         for (int k = 0; k < kGroup - 1; ++k)
-            if (k < n) s = apply(Map{from_words(m[k]), from_words(m[k] + 2)}, s);
+            if (k < n) {
+                const Map map{from_words(m[k]), from_words(m[k] + 2)};
+                s = kSeq && is_cut(map.P) ? map.q : apply(map, s);
+            }
         return s;
     }
 };
 
 // Publishes the tile's map for the later tiles of its group, or the next group's carry.
-template <typename T, bool kForward>
-__device__ __forceinline__ void publish_tile(const ScanParams<T>& p, const Map (*run)[32], Pair enter,
+template <typename T, bool kForward, bool kSeq>
+__device__ __forceinline__ void publish_tile(const ScanParams<T>& p, const Map (*run)[32], uint32_t cuts, Pair enter,
                                              const Place& w) {
     if (w.step + 1 >= p.tiles || !w.live) return;  // nobody reads it
-    Map m = run[kForward ? 0 : kWarps<T> - 1][w.lane];
+    auto nth = [](int k) { return kForward ? k : kWarps<T> - 1 - k; };  // in scan order
+    // what the runs before the last with a cut do does not count
+    const int from = !kSeq || cuts == 0u ? 0 : nth(kForward ? 31 - __clz(cuts) : __ffs(cuts) - 1);
+    Map m = run[nth(from)][w.lane];
 #pragma unroll
-    for (int k = 1; k < kWarps<T>; ++k) m = compose(run[kForward ? k : kWarps<T> - 1 - k][w.lane], m);
+    for (int k = 1; k < kWarps<T>; ++k)
+        if (!kSeq || k > from) m = compose(run[nth(k)][w.lane], m);
+    if (kSeq && cuts != 0u) m.P = cut_P();
     const long long cells = static_cast<long long>(p.batch) * p.pitch;
     if (w.step % kGroup == kGroup - 1) {
         uint32_t o[2];
-        to_words(apply(m, enter), o);
+        to_words(kSeq && cuts != 0u ? m.q : apply(m, enter), o);
         publish(p.carry + (w.step / kGroup + 1) * cells + w.cell, o);
     } else {
         uint32_t o[4];
@@ -335,7 +396,7 @@ __device__ __forceinline__ void store_sums(const ScanParams<T>& p, const Exchang
     }
 }
 
-template <typename T, bool kAny, bool kForward>
+template <typename T, bool kAny, bool kForward, bool kSeq>
 __device__ __forceinline__ void guide(const ScanParams<T>& p, Exchange<T>& ex) {
     const int lane = threadIdx.x & 31;
     // The next ticket; a sequence of one tile has nothing to take in order.
@@ -344,7 +405,7 @@ __device__ __forceinline__ void guide(const ScanParams<T>& p, Exchange<T>& ex) {
         if (p.tiles == 1) return nth++ == 0 ? static_cast<int>(blockIdx.x) : p.chains;
         return lane == 0 ? static_cast<int>(atomicAdd(p.ticket, 1u) + 1u) : 0;
     };
-    Lookup<T, kAny, kForward> next;
+    Lookup<T, kAny, kForward, kSeq> next;
     Incoming<T, kAny> in;
     for (int k = 0; k < 3; ++k) {
         next.fetch(p, __shfl_sync(0xffffffffu, ask(), 0), lane);
@@ -354,6 +415,7 @@ __device__ __forceinline__ void guide(const ScanParams<T>& p, Exchange<T>& ex) {
     unsigned i = 0;
     for (; ex.slot[i % kSlots].step >= 0; ++i) {
         const Place w = place_in<T, kAny>(p, ex.slot[i % kSlots]);
+        const uint32_t cuts = kSeq ? ex.slot[i % kSlots].cut_runs : 0u;
         const int ticket = ask();  // in flight until the tile is done
         in.start(p, w);
         // The map goes out as soon as the runs are there, whatever this tile still waits
@@ -367,10 +429,10 @@ __device__ __forceinline__ void guide(const ScanParams<T>& p, Exchange<T>& ex) {
             for (int k = 0; k < 8 && !runs; ++k) {
                 runs = ptx::mbar_test_wait(&ex.runs_ready[i & 1], i >> 1 & 1);
                 runs = __any_sync(0xffffffffu, runs);
-                if (runs && !last) publish_tile<T, kForward>(p, ex.run[i & 1], enter, w);
+                if (runs && !last) publish_tile<T, kForward, kSeq>(p, ex.run[i & 1], cuts, enter, w);
             }
             if (!entered && __all_sync(0xffffffffu, in.there())) {
-                enter = in.value(p, w);
+                enter = in.template value<kSeq>(p, w);
                 ex.enter[i & 1][lane] = enter;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&ex.enter_ready[i & 1]);
@@ -393,7 +455,7 @@ __device__ __forceinline__ void guide(const ScanParams<T>& p, Exchange<T>& ex) {
             }
             if (!entered) in.read();
         }
-        if (last) publish_tile<T, kForward>(p, ex.run[i & 1], enter, w);
+        if (last) publish_tile<T, kForward, kSeq>(p, ex.run[i & 1], cuts, enter, w);
         next.fetch(p, __shfl_sync(0xffffffffu, ticket, 0), lane);
         next.store(ex.slot[(i + 3) % kSlots], lane);
         if (!kForward && i > 0) store_sums<T, kAny>(p, ex, place_in<T, kAny>(p, ex.slot[(i - 1) % kSlots]), (i - 1) & 1);
@@ -495,14 +557,10 @@ __device__ __forceinline__ void walk_tiles(Exchange<T>& ex, Load load, Body body
     if (!kForward && i > 0) __syncthreads();  // the last tile's sums
 }
 
-// Bits r < kRun set where the state restarts at token t0 + r.
-template <int kRun>
-__device__ __forceinline__ uint32_t restarts(const int* seq, long long row, long long t0, long long L, int lane) {
-    if (!seq) return 0u;
-    const long long t = t0 + lane;
-    bool cut = false;
-    if (lane < kRun && t > 0 && t < L) cut = __ldg(seq + row * L + t) != __ldg(seq + row * L + t - 1);
-    return __ballot_sync(0xffffffffu, cut);
+// Bits r < kRun set where a sequence begins with token r of this warp's run.
+template <int kRun, bool kSeq>
+__device__ __forceinline__ uint32_t begins_in(const Slot& t, int warp) {
+    return kSeq ? t.begins[warp * kRun / 32] >> warp * kRun % 32 & ((1u << kRun) - 1u) : 0u;
 }
 
 // The decay e^(delta A) from v = delta A, for bf16 io from v = delta A log2(e). The forward of bf16 io takes the hardware's 2^x as it is (final states are
@@ -517,7 +575,7 @@ __device__ __forceinline__ Pair decay(Pair v) {
 }
 
 // kWhole: every token of the tile exists.
-template <typename T, bool kAny, bool kWhole>
+template <typename T, bool kAny, bool kSeq, bool kWhole>
 __device__ __forceinline__ bool forward_tile(const ScanParams<T>& p, Exchange<T>& ex, const Slot& t, const T* sx,
                                              const T* sd, int nth) {
     using L = Pair;
@@ -544,22 +602,22 @@ __device__ __forceinline__ bool forward_tile(const ScanParams<T>& p, Exchange<T>
             }
         }
     }
-    if (const uint32_t cut = restarts<kRun>(p.seq, w.b, t0, p.L, w.lane)) {
+    const uint32_t cut = begins_in<kRun, kSeq>(t, w.warp);
+    auto begun = [&](int r) { return (cut & ((2u << r) - 1u)) != 0u; };  // a sequence, by token r of the run
+    with<kSeq>(cut != 0u, [&](auto some) {
 #pragma unroll
-        for (int r = 0; r < kRun; ++r)
-            if (cut >> r & 1u) P[r] = L::splat(0.f);
-    }
-#pragma unroll
-    for (int r = 1; r < kRun; ++r) {
-        h[r] = elem::fma(P[r], h[r - 1], h[r]);
-        P[r] = elem::mul(P[r], P[r - 1]);
-    }
+        for (int r = 0; r < kRun; ++r) {
+            if (r > 0 && !(some.value && (cut >> r & 1u))) h[r] = elem::fma(P[r], h[r - 1], h[r]);
+            if (r > 0) P[r] = elem::mul(P[r], P[r - 1]);  // (past a cut: not used)
+        }
+    });
     const Map(*run)[32] = ex.run[turn];
     ex.run[turn][w.warp][w.lane] = {P[kRun - 1], h[kRun - 1]};
     if (!wait_enter(p, ex, nth)) return false;
     if (!w.live) return true;
-    L s = ex.enter[turn][w.lane];
-    for (int k = 0; k < w.warp; ++k) s = apply(run[k][w.lane], s);
+    const int last = kSeq ? last_before(t.cut_runs, w.warp) : -1;
+    L s = last >= 0 ? run[last][w.lane].q : ex.enter[turn][w.lane];
+    for (int k = last + 1; k < w.warp; ++k) s = apply(run[k][w.lane], s);
     // the state entering token t0 + keep_at is saved (kState<T> may end inside a run)
     int keep_at = -1;
     float* keep = nullptr;
@@ -570,16 +628,18 @@ __device__ __forceinline__ bool forward_tile(const ScanParams<T>& p, Exchange<T>
         if (keep_at == 0) store_pair<kAny>(keep, s, w.both);
     }
     const L D = t.D[w.lane];
-    T* py = p.y + row0 * p.dim + w.c;
+    with<kSeq>(cut != 0u, [&](auto some) {
+        T* py = p.y + row0 * p.dim + w.c;
 #pragma unroll
-    for (int r = 0; r < kRun; ++r, py += p.dim) {
-        if (kWhole || r < n) {
-            const L ht = elem::fma(P[r], s, h[r]);
-            store_out<T, kAny>(py, elem::fma(D, x(r), ht), w.both);
-            if (r + 1 < kRun && r + 1 == keep_at) store_pair<kAny>(keep, ht, w.both);
-            if ((!kWhole || r == kRun - 1) && p.fin && t0 + r == p.L - 1) store_pair<kAny>(p.fin + w.own, ht, w.both);
+        for (int r = 0; r < kRun; ++r, py += p.dim) {
+            if (kWhole || r < n) {
+                const L ht = some.value && begun(r) ? h[r] : elem::fma(P[r], s, h[r]);
+                store_out<T, kAny>(py, elem::fma(D, x(r), ht), w.both);
+                if (r + 1 < kRun && r + 1 == keep_at) store_pair<kAny>(keep, ht, w.both);
+                if ((!kWhole || r == kRun - 1) && p.fin && t0 + r == p.L - 1) store_pair<kAny>(p.fin + w.own, ht, w.both);
+            }
         }
-    }
+    });
     return true;
 }
 
@@ -588,7 +648,7 @@ __host__ __device__ constexpr int stage_bytes(int run, int inputs) {
     return inputs * run * kWarps<T> * kPitch<T, kAny> * static_cast<int>(sizeof(T));
 }
 
-template <typename T, bool kAny>
+template <typename T, bool kAny, bool kSeq>
 __global__ void __launch_bounds__(kThreads<T>, kCtasPerSm<T>) gated_scan_fwd(const ScanParams<T> p) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int kRun = kRunFwd<T>, kTile = kRun * kWarps<T>, kElems = kTile * kPitch<T, kAny>;
@@ -602,7 +662,7 @@ __global__ void __launch_bounds__(kThreads<T>, kCtasPerSm<T>) gated_scan_fwd(con
         ptx::fence_mbar_init();
     }
     if (warp == kWarps<T>) {
-        guide<T, kAny, true>(p, ex);
+        guide<T, kAny, true, kSeq>(p, ex);
         return;
     }
     T* mine = reinterpret_cast<T*>(smem) + warp * kRun * kPitch<T, kAny>;  // this warp's rows
@@ -618,13 +678,13 @@ __global__ void __launch_bounds__(kThreads<T>, kCtasPerSm<T>) gated_scan_fwd(con
         [&](const Slot& t, int nth) {
             const T* sx = mine + (nth & 1) * 2 * kElems;
             if (static_cast<long long>(t.step + 1) * kTile <= p.L)
-                return forward_tile<T, kAny, true>(p, ex, t, sx, sx + kElems, nth);
+                return forward_tile<T, kAny, kSeq, true>(p, ex, t, sx, sx + kElems, nth);
             else
-                return forward_tile<T, kAny, false>(p, ex, t, sx, sx + kElems, nth);
+                return forward_tile<T, kAny, kSeq, false>(p, ex, t, sx, sx + kElems, nth);
         });
 }
 
-template <typename T, bool kAny, bool kWhole>
+template <typename T, bool kAny, bool kSeq, bool kWhole>
 __device__ __forceinline__ bool backward_tile(const ScanParams<T>& p, Exchange<T>& ex, const Slot& t, const T* sx,
                                               const T* sd, const T* sg, int nth) {
     using L = Pair;
@@ -653,60 +713,63 @@ __device__ __forceinline__ bool backward_tile(const ScanParams<T>& p, Exchange<T
             }
         }
     }
-    if (const uint32_t cut = restarts<kRun>(p.seq, w.b, t0, p.L, w.lane)) {
-#pragma unroll
-        for (int r = 0; r < kRun; ++r)
-            if (cut >> r & 1u) a[r] = L::splat(0.f);
-    }
+    const uint32_t cut = begins_in<kRun, kSeq>(t, w.warp);
+    auto begins = [&](int r) { return (cut >> r & 1u) != 0u; };  // a sequence, with token r of the run
     // the run's two maps: the state's (P, f) forward in time, g's (P, q) backward
-    {
+    with<kSeq>(cut != 0u, [&](auto some) {
         L f = L::splat(0.f), P = L::splat(1.f), q = L::splat(0.f);
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
             if (kWhole || r < n) {
-                f = elem::fma(a[r], f, elem::mul(delta[r], x(r)));
+                const L in = elem::mul(delta[r], x(r));
+                f = some.value && begins(r) ? in : elem::fma(a[r], f, in);
                 P = elem::mul(P, a[r]);
             }
         }
 #pragma unroll
         for (int r = kRun - 1; r >= 0; --r)
-            if (kWhole || r < n) q = elem::mul(a[r], elem::add(q, dy(r)));
+            if (kWhole || r < n) q = some.value && begins(r) ? L::splat(0.f) : elem::mul(a[r], elem::add(q, dy(r)));
         ex.run[turn][w.warp][w.lane] = {P, q};
         ex.f[turn][w.warp][w.lane] = f;
-    }
+    });
     if (!wait_enter(p, ex, nth)) return false;
     const Map(*run)[32] = ex.run[turn];
-    // h entering the run, then h before each of its tokens
-    L h = t.state[w.lane];
-    for (int k = 0; k < w.warp; ++k) h = elem::fma(run[k][w.lane].P, h, ex.f[turn][k][w.lane]);
+    // h entering the run, then h before each of its tokens (zero before a sequence's first)
+    const int last = kSeq ? last_before(t.cut_runs, w.warp) : -1;
+    L h = last >= 0 ? ex.f[turn][last][w.lane] : t.state[w.lane];
+    for (int k = last + 1; k < w.warp; ++k) h = elem::fma(run[k][w.lane].P, h, ex.f[turn][k][w.lane]);
     L before[kRun];
 #pragma unroll
     for (int r = 0; r < kRun; ++r) {
+        if (kSeq && begins(r)) h = L::splat(0.f);
         before[r] = h;
         if (kWhole || r < n) h = elem::fma(a[r], h, elem::mul(delta[r], x(r)));
     }
     // what enters the run from the tokens after it
-    L k = ex.enter[turn][w.lane];
-    for (int o = kWarps<T> - 1; o > w.warp; --o) k = apply(run[o][w.lane], k);
+    const int next = kSeq ? first_after(t.cut_runs, w.warp) : -1;
+    L k = next >= 0 ? run[next][w.lane].q : ex.enter[turn][w.lane];
+    for (int o = (next >= 0 ? next : kWarps<T>) - 1; o > w.warp; --o) k = apply(run[o][w.lane], k);
     const L D = t.D[w.lane];
     L sA = L::splat(0.f), sb = sA, sD = sA;
-    T *px = p.y + (row0 + kRun - 1) * p.dxs + w.c, *pd = p.ddt + (row0 + kRun - 1) * p.ddts + w.c;
+    with<kSeq>(cut != 0u, [&](auto some) {
+        T *px = p.y + (row0 + kRun - 1) * p.dxs + w.c, *pd = p.ddt + (row0 + kRun - 1) * p.ddts + w.c;
 #pragma unroll
-    for (int r = kRun - 1; r >= 0; --r, px -= p.dxs, pd -= p.ddts) {
-        if (!kWhole && r >= n) continue;
-        const L dyv = dy(r), xv = x(r);
-        const L g = elem::add(dyv, k);
-        k = elem::mul(a[r], g);
-        const L gh = elem::mul(k, before[r]);  // dL / d(delta A)
-        const L dd = elem::mul(elem::fma(A, gh, elem::mul(g, xv)), slope[r]);
-        if (w.live) {
-            store_out<T, kAny>(px, elem::fma(g, delta[r], elem::mul(D, dyv)), w.both);
-            store_out<T, kAny>(pd, dd, w.both);
+        for (int r = kRun - 1; r >= 0; --r, px -= p.dxs, pd -= p.ddts) {
+            if (!kWhole && r >= n) continue;
+            const L dyv = dy(r), xv = x(r);
+            const L g = elem::add(dyv, k);
+            k = some.value && begins(r) ? L::splat(0.f) : elem::mul(a[r], g);
+            const L gh = elem::mul(k, before[r]);  // dL / d(delta A)
+            const L dd = elem::mul(elem::fma(A, gh, elem::mul(g, xv)), slope[r]);
+            if (w.live) {
+                store_out<T, kAny>(px, elem::fma(g, delta[r], elem::mul(D, dyv)), w.both);
+                store_out<T, kAny>(pd, dd, w.both);
+            }
+            sA = elem::fma(gh, delta[r], sA);
+            sb = elem::add(sb, dd);
+            sD = elem::fma(dyv, xv, sD);
         }
-        sA = elem::fma(gh, delta[r], sA);
-        sb = elem::add(sb, dd);
-        sD = elem::fma(dyv, xv, sD);
-    }
+    });
     if (p.fin && w.live && tile == 0 && w.warp == 0) store_pair<kAny>(p.fin + w.own, k, w.both);
     ex.sums[turn][0][w.warp][w.lane] = sA;
     ex.sums[turn][1][w.warp][w.lane] = sb;
@@ -714,7 +777,7 @@ __device__ __forceinline__ bool backward_tile(const ScanParams<T>& p, Exchange<T
     return true;
 }
 
-template <typename T, bool kAny>
+template <typename T, bool kAny, bool kSeq>
 __global__ void __launch_bounds__(kThreads<T>, kCtasPerSm<T>) gated_scan_bwd(const ScanParams<T> p) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int kRun = kRunBwd, kElems = kState<T> * kPitch<T, kAny>;
@@ -728,7 +791,7 @@ __global__ void __launch_bounds__(kThreads<T>, kCtasPerSm<T>) gated_scan_bwd(con
         ptx::fence_mbar_init();
     }
     if (warp == kWarps<T>) {
-        guide<T, kAny, false>(p, ex);
+        guide<T, kAny, false, kSeq>(p, ex);
         return;
     }
     T* mine = reinterpret_cast<T*>(smem) + warp * kRun * kPitch<T, kAny>;
@@ -745,9 +808,9 @@ __global__ void __launch_bounds__(kThreads<T>, kCtasPerSm<T>) gated_scan_bwd(con
         [&](const Slot& t, int nth) {
             const T* sx = mine + (nth & 1) * 3 * kElems;
             if (static_cast<long long>(p.tiles - t.step) * kState<T> <= p.L)
-                return backward_tile<T, kAny, true>(p, ex, t, sx, sx + kElems, sx + 2 * kElems, nth);
+                return backward_tile<T, kAny, kSeq, true>(p, ex, t, sx, sx + kElems, sx + 2 * kElems, nth);
             else
-                return backward_tile<T, kAny, false>(p, ex, t, sx, sx + kElems, sx + 2 * kElems, nth);
+                return backward_tile<T, kAny, kSeq, false>(p, ex, t, sx, sx + kElems, sx + 2 * kElems, nth);
         });
 }
 
@@ -841,7 +904,7 @@ ssd_status check_scan(const ssd_scan_dims* d, ssd_dtype io) {
     return SSD_OK;
 }
 
-template <typename T, bool kAny>
+template <typename T, bool kAny, bool kSeq>
 ssd_status launch_scan(ScanParams<T>& p, const ssd_scan_dims& d, bool backward, const ScanLayout& l, void* ws,
                        float* dA, float* dbias, float* dD, cudaStream_t stream) {
     p.L = d.seqlen;
@@ -863,7 +926,7 @@ ssd_status launch_scan(ScanParams<T>& p, const ssd_scan_dims& d, bool backward, 
     using Ex = Exchange<T>;
     const int smem = 2 * stage_bytes<T, kAny>(run, backward ? 3 : 2) +
                      static_cast<int>(backward ? sizeof(Ex) : offsetof(Ex, f));
-    auto* kernel = backward ? gated_scan_bwd<T, kAny> : gated_scan_fwd<T, kAny>;
+    auto* kernel = backward ? gated_scan_bwd<T, kAny, kSeq> : gated_scan_fwd<T, kAny, kSeq>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return SSD_ERR_CUDA;
     // one tile per CTA where a sequence is one tile (nothing to take in order); else persistent CTAs
@@ -879,7 +942,7 @@ ssd_status launch_scan(ScanParams<T>& p, const ssd_scan_dims& d, bool backward, 
     return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
-// Whether every row of every io tensor starts on 16 bytes.
+// Whether every row of every io tensor starts on 16 bytes, and whether sequences are packed.
 template <typename T>
 ssd_status dispatch_scan(ScanParams<T>& p, const ssd_scan_dims& d, bool backward, void* ws, size_t ws_bytes, float* dA,
                          float* dbias, float* dD, cudaStream_t stream) {
@@ -892,8 +955,9 @@ ssd_status dispatch_scan(ScanParams<T>& p, const ssd_scan_dims& d, bool backward
                           static_cast<const void*>(p.ddt)})
         wide = wide && aligned_to(q, 16);
     if (backward) wide = wide && whole(p.dys) && whole(p.dxs) && whole(p.ddts);
-    return wide ? launch_scan<T, false>(p, d, backward, l, ws, dA, dbias, dD, stream)
-                : launch_scan<T, true>(p, d, backward, l, ws, dA, dbias, dD, stream);
+    auto* launch = p.seq ? (wide ? launch_scan<T, false, true> : launch_scan<T, true, true>)
+                         : (wide ? launch_scan<T, false, false> : launch_scan<T, true, false>);
+    return launch(p, d, backward, l, ws, dA, dbias, dD, stream);
 }
 
 bool scan_aligned(ssd_dtype io, std::initializer_list<const void*> io_ptrs, std::initializer_list<const void*> f32_ptrs) {

@@ -388,3 +388,53 @@ def test_decays_above_one(io):
         bound = (2 * L + 32) * 2.0 ** -21 * most["y"][:, i] + r * ref["y"][:, i].abs()
         assert ((y.double() - ref["y"][:, i]).abs() <= bound).all()
     assert ((state.double() - ref["final_state"]).abs() <= (2 * L + 32) * 2.0 ** -21 * most["final_state"]).all()
+
+
+def plant(t, row, at, channel, what, value):
+    """A copy of t with one entry of x, dt or dy replaced."""
+    s = dict(t)
+    s[what] = t[what].clone()
+    s[what][row, at, channel] = value
+    return s
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("shape,gap", [((2, 700, 70), 90), ((1, 2500, 33), 400), ((2, 130, 64), 1)])
+def test_nothing_crosses_packed_sequences(shape, gap, io):
+    """Infinities and NaN in one sequence, in its initial state or its final gradient, change nothing in the row's
+    other sequences, forward or backward, nor in other channels: bit for bit."""
+    b, L, d = shape
+    t = make(b, L, d, DTYPES[io], seed=21)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    cuts = torch.ones(b, L, device="cuda") if gap == 1 else torch.rand(b, L, generator=g, device="cuda") < 1.0 / gap
+    cuts[:, [7, 8, 64, L // 2, L - 40]] = 1  # a sequence of one token, the first of a run, one that ends early
+    t["seq"] = torch.cumsum(cuts.int(), 1, dtype=torch.int32)
+    want = run(t)
+    row, c = b - 1, d - 2
+
+    def same(got, first, last, what):
+        """Everything but channel c of the sequence at tokens [first, last], and the sums over it."""
+        for k in ("y", "dx", "ddt"):
+            kept = torch.ones_like(got[k], dtype=torch.bool)
+            kept[row, first:last + 1, c] = False
+            assert torch.equal(got[k][kept], want[k][kept]), f"{what}: {k}"
+        for k, owner in (("final_state", L - 1), ("dinit_state", 0)):
+            kept = torch.ones_like(got[k], dtype=torch.bool)
+            kept[row, c] = not first <= owner <= last
+            assert torch.equal(got[k][kept], want[k][kept]), f"{what}: {k}"
+        kept = torch.arange(d, device="cuda") != c
+        for k in ("ddt_bias", "dA", "dD"):
+            assert torch.equal(got[k][kept], want[k][kept]), f"{what}: {k}"
+
+    seq = t["seq"][row].tolist()
+    for at in (0, 6, 7, 8, 63, 64, 70, L // 2 - 1, L // 2, L - 41, L - 40, L - 1):
+        first, last = seq.index(seq[at]), L - 1 - seq[::-1].index(seq[at])
+        for what, value in (("x", math.inf), ("x", math.nan), ("dt", math.nan), ("dy", -math.inf), ("dy", math.nan)):
+            same(run(plant(t, row, at, c, what, value)), first, last, f"{what}[{at}] = {value}")
+    for value in (math.inf, math.nan):
+        s = dict(t, init=t["init"].clone())
+        s["init"][row, c] = value
+        same(run(s), 0, L - 1 - seq[::-1].index(seq[0]), f"initial state {value}")
+        s = dict(t, dfin=t["dfin"].clone())
+        s["dfin"][row, c] = value
+        same(run(s), seq.index(seq[-1]), L - 1, f"final gradient {value}")
