@@ -563,15 +563,20 @@ __device__ __forceinline__ uint32_t begins_in(const Slot& t, int warp) {
     return kSeq ? t.begins[warp * kRun / 32] >> warp * kRun % 32 & ((1u << kRun) - 1u) : 0u;
 }
 
-// The decay e^(delta A) from v = delta A, for bf16 io from v = delta A log2(e). The forward of bf16 io takes the hardware's 2^x as it is (final states are
-// 4e-7 off, far inside y's rounding; exp_near costs it 13 % of its time); fp32 io and
-// the gradients, whose fp32 sums over tokens keep such errors, do not.
-template <typename T>
-__device__ __forceinline__ Pair decay(Pair v) {
+// The decay e^(delta A), from delta and A_in = decay_A(A). The forward and the decode step of bf16 io take the
+// hardware's 2^x as it is, with A in units of log 2 (final states are 4e-7 off, far inside y's rounding; exp_near
+// costs the forward 13 % of its time); fp32 io and the gradients, whose states and sums over tokens keep such
+// errors, do not (4000 fp32 decode steps with decays down to 1 - 1/2000: 1e-5 off by 2^x, 1.4e-6 so).
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> decay_A(Vals<V> A) {
+    return sizeof(T) == 2 ? elem::mul(A, Vals<V>::splat(elem::kLog2e)) : A;
+}
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> decay(Vals<V> A_in, Vals<V> delta) {
     if constexpr (sizeof(T) == 2)
-        return elem::exp2_fast<2>(v);
+        return elem::exp2_fast<V>(elem::mul(A_in, delta));
     else
-        return elem::exp_near<2>(v);
+        return elem::exp_near<V>(elem::mul(A_in, delta));
 }
 
 // kWhole: every token of the tile exists.
@@ -589,15 +594,14 @@ __device__ __forceinline__ bool forward_tile(const ScanParams<T>& p, Exchange<T>
     // per token: decay and input; then the run's map token by token: h_t from a zero state, decay product P_t
     L h[kRun], P[kRun];
     {
-        // (bf16: A in units of log 2, see decay)
-        const L A = sizeof(T) == 2 ? elem::mul(t.A[w.lane], L::splat(elem::kLog2e)) : t.A[w.lane], bias = t.bias[w.lane];
+        const L A = decay_A<T, 2>(t.A[w.lane]), bias = t.bias[w.lane];
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
             P[r] = L::splat(1.f), h[r] = L::splat(0.f);
             if (kWhole || r < n) {
                 L u;
                 const L delta = elem::softplus<2>(elem::add(dt(r), bias), &u);
-                P[r] = decay<T>(elem::mul(A, delta));
+                P[r] = decay<T, 2>(A, delta);
                 h[r] = elem::mul(delta, x(r));
             }
         }
@@ -854,7 +858,7 @@ __global__ void __launch_bounds__(128)
     dv.load(dt + b * dts + c);
     L u;
     const L delta = elem::softplus<V>(elem::add(elem::unpack<T, V>(dv), L::load(bias + c)), &u);
-    const L a = elem::exp2_fast<V>(elem::mul(elem::mul(L::load(A + c), L::splat(elem::kLog2e)), delta));
+    const L a = decay<T, V>(decay_A<T, V>(L::load(A + c)), delta);
     const L h = elem::fma(a, L::load(state + b * dim + c), elem::mul(delta, elem::unpack<T, V>(xv)));
     h.store(state + b * dim + c);
     elem::store_vals<T, V>(y + b * dim + c, D ? elem::fma(L::load(D + c), elem::unpack<T, V>(xv), h) : h);

@@ -438,3 +438,29 @@ def test_nothing_crosses_packed_sequences(shape, gap, io):
         s = dict(t, dfin=t["dfin"].clone())
         s["dfin"][row, c] = value
         same(run(s), seq.index(seq[-1]), L - 1, f"final gradient {value}")
+
+
+@pytest.mark.parametrize("vary", [False, True])
+def test_slow_decays_in_fp32(vary):
+    """Decode steps and the scan of thousands of slow tokens. A decay near one carries 2^-24 (its rounding, and delta's
+    2^-22 of an exponent below 2^-8) and a state's update 2^-24, each kept for about T = 1 / (1 - a) tokens; inputs
+    are positive, so the state itself bounds the sum: 2^-23 T of it. Gates that vary make the roundings independent: a
+    decay's is uniform within 2^-25 and an update's within 2^-24, 2^-24.5 together in the mean square at most, over T / 2
+    tokens (a^2 in the place of a): six standard deviations are 6 2^-24.5 sqrt(T / 2)."""
+    import mamba_ssd_chunked_gb300 as pkg
+    b, L, d = 1, 4000, 96
+    t = make(b, L, d, torch.float32, seed=23, with_D=False)
+    t["x"], t["init"] = t["x"].abs() + 0.1, t["init"].abs()
+    t["dt"] *= 0.1 if vary else 0.0
+    slow = torch.linspace(1.0 / 300, 1.0 / 2000, d, device="cuda").double()  # delta |A|, 1 / T
+    t["A"] = -torch.ones(d, device="cuda")
+    t["dt_bias"] = torch.log(torch.expm1(slow)).float()
+    ref = reference(t)["final_state"]
+    bound = ref * (6 * 2.0 ** -24.5 * torch.sqrt(0.5 / slow) if vary else 2.0 ** -23 / slow)
+    fin = run(t)["final_state"]
+    state = t["init"].clone()
+    for i in range(L):
+        pkg.ssd_gated_scan_step(t["x"][:, i], t["dt"][:, i], t["dt_bias"], t["A"], state=state)
+    for what, got in (("scan", fin), ("steps", state)):
+        worst = ((got.double() - ref).abs() / bound).max().item()
+        assert worst <= 1.0, f"{what}: {worst:.2f} of the bound"
