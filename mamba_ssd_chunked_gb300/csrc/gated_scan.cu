@@ -181,8 +181,8 @@ __device__ __forceinline__ Pair apply(Map m, Pair s) {
 // the decay would not do: zero times an infinity or a NaN of the other sequence is NaN. A run with such a
 // token (Slot::cut_runs) maps every s to q, and maps are composed from the last such run on; a published
 // tile's P is then -0, which no product of decays is (none of them is negative). The guide looks seq_idx up
-// with the tile. 4 x 4096 x 5120 (bf16) in sequences of 300 tokens: forward 134 us (126 unpacked), backward 279 (252);
-// 1 x 131072 x 4096: 787 (736) and 1735 (1555).
+// with the tile. 4 x 4096 x 5120 (bf16) in sequences of 300 tokens: forward 135 us (125 unpacked), backward 279 (255);
+// 1 x 131072 x 4096: 792 (731) and 1727 (1573).
 __device__ __forceinline__ Pair cut_P() { return Pair::splat(-0.f); }
 __device__ __forceinline__ bool is_cut(Pair P) { return __float_as_uint(P.get(0)) == 0x80000000u; }  // (both channels alike)
 // f(std::true_type) or f(std::false_type); kMay: `yes` may be true
@@ -192,6 +192,11 @@ __device__ __forceinline__ void with(bool yes, F f) {
         f(std::true_type{});
     else
         f(std::false_type{});
+}
+// and with two conditions
+template <bool kMay, typename F>
+__device__ __forceinline__ void with(bool yes, bool second, F f) {
+    with<kMay>(yes, [&](auto a) { with<true>(second, [&](auto b) { f(a, b); }); });
 }
 
 // A tile as the computing warps see it, looked up three tiles ahead by the guiding warp.
@@ -632,13 +637,13 @@ __device__ __forceinline__ bool forward_tile(const ScanParams<T>& p, Exchange<T>
         if (keep_at == 0) store_pair<kAny>(keep, s, w.both);
     }
     const L D = t.D[w.lane];
-    with<kSeq>(cut != 0u, [&](auto some) {
+    with<kSeq>(cut != 0u, p.D != nullptr, [&](auto some, auto skip) {  // (zero times an infinite x is no skip)
         T* py = p.y + row0 * p.dim + w.c;
 #pragma unroll
         for (int r = 0; r < kRun; ++r, py += p.dim) {
             if (kWhole || r < n) {
                 const L ht = some.value && begun(r) ? h[r] : elem::fma(P[r], s, h[r]);
-                store_out<T, kAny>(py, elem::fma(D, x(r), ht), w.both);
+                store_out<T, kAny>(py, skip.value ? elem::fma(D, x(r), ht) : ht, w.both);
                 if (r + 1 < kRun && r + 1 == keep_at) store_pair<kAny>(keep, ht, w.both);
                 if ((!kWhole || r == kRun - 1) && p.fin && t0 + r == p.L - 1) store_pair<kAny>(p.fin + w.own, ht, w.both);
             }
@@ -755,7 +760,7 @@ __device__ __forceinline__ bool backward_tile(const ScanParams<T>& p, Exchange<T
     for (int o = (next >= 0 ? next : kWarps<T>) - 1; o > w.warp; --o) k = apply(run[o][w.lane], k);
     const L D = t.D[w.lane];
     L sA = L::splat(0.f), sb = sA, sD = sA;
-    with<kSeq>(cut != 0u, [&](auto some) {
+    with<kSeq>(cut != 0u, p.D != nullptr, [&](auto some, auto skip) {
         T *px = p.y + (row0 + kRun - 1) * p.dxs + w.c, *pd = p.ddt + (row0 + kRun - 1) * p.ddts + w.c;
 #pragma unroll
         for (int r = kRun - 1; r >= 0; --r, px -= p.dxs, pd -= p.ddts) {
@@ -766,7 +771,7 @@ __device__ __forceinline__ bool backward_tile(const ScanParams<T>& p, Exchange<T
             const L gh = elem::mul(k, before[r]);  // dL / d(delta A)
             const L dd = elem::mul(elem::fma(A, gh, elem::mul(g, xv)), slope[r]);
             if (w.live) {
-                store_out<T, kAny>(px, elem::fma(g, delta[r], elem::mul(D, dyv)), w.both);
+                store_out<T, kAny>(px, skip.value ? elem::fma(g, delta[r], elem::mul(D, dyv)) : elem::mul(g, delta[r]), w.both);
                 store_out<T, kAny>(pd, dd, w.both);
             }
             sA = elem::fma(gh, delta[r], sA);

@@ -464,3 +464,19 @@ def test_slow_decays_in_fp32(vary):
     for what, got in (("scan", fin), ("steps", state)):
         worst = ((got.double() - ref).abs() / bound).max().item()
         assert worst <= 1.0, f"{what}: {worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_infinities_without_a_skip(io):
+    """Without D nothing multiplies x or dy but the recurrence: an infinite input gives infinite outputs, as in a decode
+    step, where zero times infinity would be NaN."""
+    import mamba_ssd_chunked_gb300 as pkg
+    t = make(1, 300, 34, DTYPES[io], seed=24, with_D=False)
+    t["dt_bias"].fill_(0.0)
+    t["A"].fill_(-1e-3)
+    t["x"][0, 200, 3], t["dy"][0, 100, 5] = math.inf, -math.inf
+    got = run(t)
+    assert (got["y"][0, 200:, 3] == math.inf).all() and torch.isfinite(got["y"][0, :200]).all()
+    assert (got["dx"][0, :101, 5] == -math.inf).all() and torch.isfinite(got["dx"][0, 101:]).all()
+    y = pkg.ssd_gated_scan_step(t["x"][:, 200], t["dt"][:, 200], t["dt_bias"], t["A"], state=t["init"].clone())
+    assert y[0, 3] == math.inf
