@@ -314,6 +314,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What exponents are taken relative to: the maximum, or nothing while there is none (no class so far, or
+// only logits of minus infinity: they count zero; of NaN: the sum is NaN).
+__device__ __forceinline__ float relative_to(float m) { return m == -__builtin_inff() ? 0.f : m; }
+
 __device__ __forceinline__ void epilogue_stats(const EpiTile& e) {
     const CeParams& p = e.p;
     const long long col0 = p.v0 + static_cast<long long>(e.t.n) * kTileN + e.half * kEpiCols;
@@ -336,10 +340,11 @@ __device__ __forceinline__ void epilogue_stats(const EpiTile& e) {
 #pragma unroll
         for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(r[i]));
         const float m2 = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+        const float base = relative_to(m2);
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) part[i & 3] += elem::exp2_fast((__uint_as_float(r[i]) - m2) * elem::kLog2e);
-        s = fmaf(s, elem::exp2_fast((m - m2) * elem::kLog2e), (part[0] + part[1]) + (part[2] + part[3]));
+        for (int i = 0; i < 32; ++i) part[i & 3] += elem::exp2_fast((__uint_as_float(r[i]) - base) * elem::kLog2e);
+        s = fmaf(s, elem::exp2_fast((m - base) * elem::kLog2e), (part[0] + part[1]) + (part[2] + part[3]));
         m = m2;
         const int at = within64(target - (col0 + c));
         if (at >= 0 && at < 32) {
@@ -720,9 +725,8 @@ __global__ void __launch_bounds__(kLseRows * kLseGroups)
 #pragma unroll 4
             for (int t = group; t < parts; t += kLseGroups) {
                 const float2 v = stats[t * rows + row];
-                const float m2 = fmaxf(m, v.x);
-                if (m2 == -__builtin_inff()) continue;  // half a tile past the vocabulary
-                s = s * elem::exp2_fast((m - m2) * elem::kLog2e) + v.y * elem::exp2_fast((v.x - m2) * elem::kLog2e);
+                const float m2 = fmaxf(m, v.x), base = relative_to(m2);  // (half a tile past the vocabulary has no maximum)
+                s = s * elem::exp2_fast((m - base) * elem::kLog2e) + v.y * elem::exp2_fast((v.x - base) * elem::kLog2e);
                 m = m2;
             }
         }
@@ -857,7 +861,7 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
     for (int off = kPer / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) s += elem::exp2_fast((v[i] - m) * elem::kLog2e);
+    for (int i = 0; i < kCols; ++i) s += elem::exp2_fast((v[i] - relative_to(m)) * elem::kLog2e);
 #pragma unroll
     for (int off = kPer / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (first == 0 && mine < rows) stats[blockIdx.x * rows + mine] = make_float2(m, s);
