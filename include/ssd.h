@@ -582,9 +582,9 @@ SSD_API ssd_status ssd_linear_cross_entropy(ssd_dtype io_dtype, int64_t rows, in
  *   dhidden = dl weight      dweight = dl^T hidden
  *
  * dloss device [rows] fp32; dhidden [rows, dim] and dweight [vocab, dim] device
- * outputs, io dtype, dense, both written whole. dl is rounded to bf16 (to three bf16
- * terms for fp32 io) as an operand of the two products; sums are fp32 and both
- * gradients are rounded once. Workspace: ssd_linear_cross_entropy_workspace_bytes(..., 1).
+ * outputs, io dtype, dense, both written whole. dl, at a target from the logit summed in
+ * fp32, is rounded to bf16 (to three bf16 terms for fp32 io) as an operand of the two products;
+ * sums are fp32 and both gradients are rounded once. Workspace: ssd_linear_cross_entropy_workspace_bytes(..., 1).
  * Errors as the forward's.
  */
 SSD_API ssd_status ssd_linear_cross_entropy_bwd(ssd_dtype io_dtype, int64_t rows, int64_t dim, int64_t vocab,

@@ -76,7 +76,7 @@ struct CeParams {
     Product prod[2];
     int jobs[2];  // tiles of each product; prod[1] only in kGrads
     int lead;     // see nth_tile
-    int late;     // reads nothing that the kernel before it writes: waits for it only at its end
+    int late;     // its operands are not written by the kernels before it: only the epilogue waits for them
     int segs;     // 1 (bf16), or the six products of three-term operands
     int seg_a[kMaxSegs], seg_b[kMaxSegs];
     long long rows, vocab, dim;
@@ -85,7 +85,7 @@ struct CeParams {
     long long ignore;
     // kStats
     float2* stats;  // [2 tiles_n, rows]: per half tile
-    float* picked;  // [rows]: the targets' logits (kDlogits: summed in fp32, or NULL)
+    float* picked;  // [rows]: the targets' logits (kDlogits: summed in fp32)
     // kDlogits
     const float* lse;
     const float* dloss;  // (and kGrads)
@@ -389,7 +389,7 @@ __device__ __forceinline__ void epilogue_dlogits(const EpiTile& e, const CUtenso
         if (at >= 0 && at < 64) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-                if (i == at) d[i] = p.picked ? g * expm1f(p.picked[e.row] - lse) : d[i] - g;
+                if (i == at) d[i] = g * expm1f(p.picked[e.row] - lse);
         }
         if (left < 64 || !kept) {  // entries past the vocabulary; rows without a loss, whatever their logits are
 #pragma unroll
@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 4) {
         // ---- epilogue: thread = row of this CTA's half of the tile, 128 of its columns
+        if (p.late) ptx::griddep_wait();
         const int sub = warp & 3, half = (warp - 4) >> 2;
         const float scale = MODE == kGrads ? reference_dloss(p.dloss) : 1.f;
         uint32_t turn = 0;
@@ -751,11 +752,13 @@ __global__ void __launch_bounds__(kLseRows * kLseGroups)
     }
 }
 
-// The targets' logits in fp32, a warp per row, for the backward of fp32 operands: a trained
-// row's p - 1 at its target is the difference of that logit and the lse, which the
-// forward took from this sum.
+// The targets' logits in fp32, a warp per row, for the backward: a trained row's p - 1 at its
+// target is the difference of that logit and the lse, which the forward took from this sum. (The
+// tensor cores' sum is off by an ulp per 16 of depth: bf16 rows of 4096 with 1 - p = 2e-3 and 3e-5 had gradients 4 %
+// and 260 % off by it, 0.2 % and 3 % so.)
+template <typename T>
 __global__ void __launch_bounds__(256)
-    ce_targets(const float* __restrict__ hidden, long long stride, const float* __restrict__ weight, long long dim, int vec,
+    ce_targets(const T* __restrict__ hidden, long long stride, const T* __restrict__ weight, long long dim, int vec,
                const long long* __restrict__ target, long long ignore, long long rows, long long vocab, float* picked) {
     ptx::griddep_launch_dependents();
     const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -1011,7 +1014,7 @@ CePlan ce_plan(long long rows, long long dim, long long vocab, ssd_dtype io, boo
         c.piece = static_cast<int>((all + pieces - 1) / pieces * kTileN);  // even pieces
         const long long tiles = up(rows, kTileM) / kTileM * (up(dim, kTileN) / kTileN);
         c.splits = static_cast<int>(std::max<long long>(1, std::min<long long>((c.planes > 1 ? 2 : 1) * pairs / tiles, c.piece / kBK / 4)));
-        c.picked = take(c.planes > 1 ? 4 * rows : 0);
+        c.picked = take(4 * rows);
         c.dl = take(2ll * c.planes * rows * c.piece);
         c.acc = take(4ll * c.splits * rows * c.ld);
     }
@@ -1217,7 +1220,7 @@ ssd_status ce_backward(const CeCall& c, const CePlan& pl, const float* dloss, co
     p.dw_vec = c.dim % (p.dw_f32 ? 4 : 8) == 0 && aligned_to(dweight, 16);
     Maps logits{}, grads{};
     // The logits come from hidden itself where they can (a row without a loss has none that count):
-    // their kernel then runs beside the packing.
+    // their products then run beside the packing and the targets' logits.
     const bool beside = in_place(c.hidden, c.hs, c) && pl.form == kInPlace;
     if (!make_map_bf16(&logits.a0, beside ? c.hidden : o.h, beside ? c.dim : o.h_ld, 1, c.rows, pl.planes, 64) ||
         !make_map_bf16(&logits.out, dl, pl.piece, 1, c.rows, pl.planes, 32) ||
@@ -1230,12 +1233,17 @@ ssd_status ce_backward(const CeCall& c, const CePlan& pl, const float* dloss, co
                                : make_map_bf16(&grads.dw, dweight, c.dim, 1, c.vocab, 1, 32)))
         return SSD_ERR_CUDA;
     logits.a1 = logits.a0;
-    if (pl.planes > 1) {
-        p.picked = reinterpret_cast<float*>(c.ws + pl.picked);
-        launch(true, ce_targets, static_cast<unsigned>((c.rows + 7) / 8), 256, 0, c.stream,
-               static_cast<const float*>(c.hidden), c.hs, static_cast<const float*>(c.weight), c.dim,
+    p.picked = reinterpret_cast<float*>(c.ws + pl.picked);
+    auto targets = [&](auto tag) {
+        using T = decltype(tag);
+        launch(true, ce_targets<T>, static_cast<unsigned>((c.rows + 7) / 8), 256, 0, c.stream,
+               static_cast<const T*>(c.hidden), c.hs, static_cast<const T*>(c.weight), c.dim,
                whole16(c.hidden, c.hs, c) && whole16(c.weight, c.dim, c), c.target, c.ignore, c.rows, c.vocab, p.picked);
-    }
+    };
+    if (c.io == SSD_BF16)
+        targets(__nv_bfloat16());
+    else
+        targets(float());
     const int tiles_r = static_cast<int>(up(c.rows, kTileM) / kTileM);
     const int tiles_d = static_cast<int>(up(c.dim, kTileN) / kTileN);
     for (long long v0 = 0; v0 < c.vocab; v0 += pl.piece) {
