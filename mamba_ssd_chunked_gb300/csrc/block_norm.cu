@@ -87,6 +87,7 @@ struct NormParams {
     int lanes;  // direct kernels: lanes per row where a row takes one warp or less (else 32)
     float eps;
     unsigned* status;
+    unsigned long long wait_ns;  // limit on a wait for a row's copies
 };
 
 // Sums N values over the threads of one row: `lanes` (8, 16 or 32) lanes of each of its warps.
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(bwd_threads(R * V)) block_norm_bwd(const NormP
 // 512 threads and 162 with 640, whose registers spill)
 constexpr int ring_threads(int V, int R, bool backward) { return V * R > 8 || (backward && V <= 2) ? 512 : 640; }
 constexpr int kRingBytes = 208 << 10;
-constexpr unsigned long long kCopyWaitNs = 2000000000ull;  // limit on a wait for a row's copies
+constexpr unsigned long long kDrainNs = 2000000000ull;  // limit on the wait for copies in flight after a wait has run out
 
 struct RingShape {
     int groups, stages;
@@ -429,6 +430,15 @@ __device__ __forceinline__ void group_sum(float (&s)[N], float* buf, int warps, 
         for (int i = 0; i < N; ++i) s[i] += buf[w * N + i];
 }
 
+// Polls for a phase for at most limit_ns.
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t phase, unsigned long long limit_ns) {
+    if (ptx::mbar_test_wait(bar, phase)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_test_wait(bar, phase))
+        if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
+    return true;
+}
+
 // Common to both directions: the group's place, its ring, and the walk over its rows.
 // body(row, stage, release): release(), called by the whole group once it has read the stage.
 template <typename T, typename TR, bool kBwd, bool kAny, typename Body>
@@ -443,23 +453,34 @@ __device__ __forceinline__ void walk_rows(const NormParams<T, TR>& p, const Ring
         ptx::fence_mbar_init();
     }
     __syncthreads();
-    const long long step = static_cast<long long>(gridDim.x) * g.groups;
-    const long long row0 = static_cast<long long>(blockIdx.x) * g.groups + group;
+    const uint32_t step = gridDim.x * g.groups, rows = static_cast<uint32_t>(p.rows);  // (sums stay below 2^32)
+    const uint32_t row0 = blockIdx.x * g.groups + group;
     const bool loader = warp == first_warp && lane == 0;
     if (loader) {
         for (int i = 0; i < g.stages; ++i)
-            if (row0 + i * step < p.rows) ring.load(i, row0 + i * step);
+            if (row0 + i * step < rows) ring.load(i, row0 + i * step);
     }
     int at = 0;
     uint32_t phase = 0;
-    for (long long row = row0; row < p.rows; row += step) {
-        if (!ptx::mbar_wait(&full[group * g.stages + at], phase, kCopyWaitNs)) {
-            atomicOr(p.status, 1u);
+    for (uint32_t row = row0; row < rows; row += step) {
+        if (!__all_sync(0xffffffffu, poll(&full[group * g.stages + at], phase, p.wait_ns))) {
+            // A warp whose wait has run out reports it and works on no more rows, but meets the other warps at the
+            // barriers of those rows (their waits end too: nothing more is copied once the loader has left). The
+            // loader first sees its copies in flight land, so that none is left when the CTA ends.
+            if (lane == 0) atomicOr(p.status, 1u);
+            for (int i = 0; i < g.stages && loader && row + i * step < rows; ++i) {
+                poll(&ring.full[at], phase, kDrainNs);
+                if (++at == g.stages) at = 0, phase ^= 1u;
+            }
+            __syncwarp();
+            const int barriers = p.warps_per_row == 1 ? 0 : !kBwd && p.pre ? 2 : 1;  // group_sums of a row
+            for (; row < rows; row += step)
+                for (int i = 0; i < barriers; ++i) ptx::named_sync(1 + group, 32 * p.warps_per_row);
             return;
         }
-        const long long next = row + g.stages * step;
+        const uint32_t next = row + g.stages * step;
         body(row, ring, ring.stage(at), [&] {
-            if (loader && next < p.rows) ring.load(at, next);
+            if (loader && next < rows) ring.load(at, next);
         });
         if (++at == g.stages) at = 0, phase ^= 1u;
     }
@@ -809,8 +830,7 @@ ssd_status launch_norm(NormParams<T, TR>& p, int align, bool backward, NormPlan*
     RingShape g;
     if (ring_plan(p, align, backward, n, &g)) {
         p.warps_per_row = n->warps_per_row;
-        unsigned long long unused;
-        const ssd_status st = call_context(&p.status, &unused);
+        const ssd_status st = call_context(&p.status, &p.wait_ns);
         if (st != SSD_OK) return st;
         return launch_ring(p, *n, g, backward, stream);
     }

@@ -335,3 +335,21 @@ def test_many_rows_with_absent_inputs(shape, drop):
         got = again()
         for k in first:
             assert torch.equal(first[k], got[k]), k
+
+
+@pytest.mark.parametrize("shape", [(3000, 2560), (3000, 2559)])
+def test_a_wait_that_runs_out_is_reported(shape, monkeypatch):
+    """With a limit of one nanosecond the persistent kernels do not see their rows arrive in time: the calls end, the
+    device status says so, and the next ones are right."""
+    import mamba_ssd_chunked_gb300 as pkg
+    t = make(*shape, torch.bfloat16, torch.float32, seed=17)
+    want = run(t)
+    assert pkg.ssd_device_status() == 0
+    monkeypatch.setenv("SSD_DEVICE_WAIT_NS", "1")
+    run(t)
+    assert pkg.ssd_device_status() == 4  # SSD_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("SSD_DEVICE_WAIT_NS")
+    got = run(t)
+    assert pkg.ssd_device_status() == 0
+    for k in want:
+        assert torch.equal(want[k], got[k]), k
