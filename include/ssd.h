@@ -445,7 +445,9 @@ typedef struct {
  *                 kept, and no other call may use it at the same time.
  *
  * State and products are fp32; only y is rounded to the io dtype. Results do
- * not depend on timing. Errors: SSD_ERR_INVALID_ARG (NULL, sizes < 1, strides
+ * not depend on timing. Rows of x, dt (and the backward's dy) that do not start on 16 bytes are read as the
+ * aligned 16-byte blocks that hold them: up to 14 bytes before a tensor's first and after its last element are
+ * read too, and not used (any cudaMalloc block may be read so far). Errors: SSD_ERR_INVALID_ARG (NULL, sizes < 1, strides
  * < dim), SSD_ERR_UNSUPPORTED (misaligned elements, sizes beyond the indexing
  * limits), SSD_ERR_WORKSPACE. Asynchronous on `stream`.
  */
@@ -513,7 +515,8 @@ SSD_API size_t ssd_gated_scan_workspace_bytes(const ssd_scan_dims* dims, ssd_dty
  * rstd            device [rows, 2] fp32 or NULL: the two 1/rms values (1 where the
  *                 norm is absent) that ssd_block_norm_bwd needs.
  *
- * out is taken from the fp32 residual, before it is rounded to residual_dtype.
+ * out is taken from the fp32 residual, before it is rounded to residual_dtype. Rows that do not start on 16
+ * bytes may be read as the aligned 16-byte blocks that hold them, as ssd_gated_scan's are.
  * dim is at most 16384. Errors: SSD_ERR_INVALID_ARG (NULL, sizes < 1, strides <
  * dim, eps < 0), SSD_ERR_UNSUPPORTED (dim or rows beyond the limits, misaligned
  * elements). Asynchronous on `stream`; no workspace.

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(bwd_threads(R * V)) block_norm_bwd(const NormP
 // Here a CTA stays on its SM and each of its groups of warps takes every n-th row: a group's first
 // lane has the next rows' tensors copied into shared memory (one bulk copy per tensor and row, a
 // ring of stages) while the group works, and the weights stay in registers.
-// 96 or 128 registers a thread (rows that start anywhere, backward: 16384 x 771 takes 100 us with
+// 96 or 128 registers a thread (rows that start anywhere, backward: 16384 x 771 took 100 us with
 // 512 threads and 162 with 640, whose registers spill)
 constexpr int ring_threads(int V, int R, bool backward) { return V * R > 8 || (backward && V <= 2) ? 512 : 640; }
 constexpr int kRingBytes = 208 << 10;
@@ -761,10 +761,10 @@ ssd_status launch_norm_v(const NormParams<T, TR>& p, const NormPlan& n, bool bac
 
 // The ring's plan. Rows on 16 bytes: one vector per thread (the forward: two over 384
 // vectors), up to 640 vectors backward and 1024 forward (16384 x 8192 forward and
-// backward: 0.94 ms with the forward on the ring and the backward direct, 1.28 ms both direct; the backward's
+// backward: 0.93 ms with the forward on the ring and the backward direct, 1.28 ms both direct; the backward's
 // two vectors per thread would spill). Rows that start anywhere: eight elements per thread, up to
 // 4096 backward and 5120 forward (both directions together, bf16 with an fp32 residual, against the
-// direct kernels: 16384 x 771 162 and 251 us, x 2561 583 and 1078, x 4001 654 and 1486; with four elements per thread
+// direct kernels: 16384 x 771 149 and 251 us, x 2561 531 and 1078, x 4001 599 and 1486; with four elements per thread
 // x 771 217). As many groups as the threads allow, at least two stages each. Other
 // rows, rows that share a warp, and too few rows to fill every group's ring on every SM take the
 // direct kernels.

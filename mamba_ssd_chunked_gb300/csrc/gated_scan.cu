@@ -54,9 +54,11 @@ using Pair = Vals<2>;  // a thread's two channels
 
 // Computing warps per CTA (consecutive runs of tokens; one more warp guides them) and
 // CTAs per SM. Registers hold 16 warps per SM either way. One CTA of 15 + 1 warps
-// against two of 7 + 1, bf16: 1 x 131072 x 4096 forward 701 against 918 us (longer
+// against two of 7 + 1, bf16, when the choice was made: 1 x 131072 x 4096 forward 701 against 918 us (longer
 // tiles: fewer steps along a sequence), 4 x 4096 x 5120 forward 121 against 117 us,
-// with the backward 366 against 360 us. The fp32 backward's stages would not fit with 15.
+// with the backward 366 against 360 us. The fp32 backward's stages would not fit with 15; with 7 they and
+// the exchange take 117 KB (122 off 16 bytes), so only one of its two CTAs is on an SM at a time (tiles go
+// by ticket, so the second half of the grid finds what is left).
 template <typename T>
 constexpr int kWarps = sizeof(T) == 2 ? 15 : 7;
 template <typename T>
@@ -488,8 +490,8 @@ __device__ __forceinline__ bool wait_enter(const ScanParams<T>& p, Exchange<T>& 
 // Elements of a 16-byte granule, and from one row of a stage to the next. Copies start on and
 // consist of granules: a row that starts anywhere arrives as the granules that hold it, one more
 // than its 64 elements fill, and begins row_shift elements into its slot. 4 x 4096 x 5121 (bf16),
-// forward and forward + backward: 180 and 541 us; in words of 4 bytes 222 and 652; in elements, one channel
-// per thread, 437 and 1214; x 5120, whose rows all start on 16 bytes, 122 and 383.
+// forward and forward + backward: 184 and 532 us; in words of 4 bytes 222 and 652; in elements, one channel
+// per thread, 437 and 1214; x 5120, whose rows all start on 16 bytes, 125 and 380.
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 template <typename T, bool kAny>

@@ -1048,8 +1048,9 @@ unsigned rows_grid(long long rows, long long ld) {
 // A call's kernels form a chain of programmatic launches: each starts while the one before it
 // drains and waits on the device for what it reads, and every one waits for the one before it
 // before it ends, so that a kernel's end means the end of all earlier ones. The
-// first starts as usual (`after`: it is not the first). Forward + backward launched one
-// after another and so: 301 x 771 x 8191 (fp32, ten kernels) 200 and 172 us, 512 x 768 x 32000 (bf16, six) 118 and 115.
+// first starts as usual (`after`: it is not the first; nor does one that overwrites what an earlier one reads). Forward +
+// backward launched one after another and so: 301 x 771 x 8191 (fp32, ten kernels) 200 and 172 us, 512 x 768 x 32000 (bf16,
+// then six) 118 and 115.
 template <typename... P, typename... A>
 void launch(bool after, void (*kernel)(P...), unsigned grid, unsigned block, int smem, cudaStream_t stream, A... args) {
     cudaLaunchAttribute attr{};
